@@ -647,6 +647,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (mt * kM + r < rows) p.ws.pml[slot * kM + r] = make_float2(m, l);
                 }
+                // the next segment's query rows land where other warps of the
+                // group have staged theirs (256 bytes a row here, two halves of
+                // 128 there): every warp, live or not, waits for the group's
+                // four.  Once per change of unit inside a run.
+                if (f < f1) asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
             } else {
                 // the two groups' parts of the same rows joined: each hands
                 // the other 64 channels and finishes the other 64.  A group
