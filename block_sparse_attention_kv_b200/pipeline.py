@@ -12,12 +12,25 @@ import torch
 from . import abi
 
 
+def _as_stream(stream, device):
+    """torch's Stream for a stream argument: a Stream, a raw handle (0: the
+    legacy default stream) or None."""
+    if not isinstance(stream, int):
+        return stream
+    if stream == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device=device)
+
+
 class DeviceLayer:
     def __init__(self, data, budget: int = None, stream=None, block_size=None,
                  fmt: int = abi.ABSP_CENTROIDS_INT4):
         """`data` is a synth.LayerData on a CUDA device; `block_size`
         overrides its per-KV-head block-size table (same cache, other
-        blocking)."""
+        blocking).  Calls run on `stream` (None: the current one).  Buffers
+        that the layer makes are ordered with it; a caller's own work on other
+        streams, and tensors it passes or reads, are the caller's to order.
+        One call of a layer at a time: its calls share workspaces."""
         self.data = data
         self.device = data.q.device
         self.budget = int(budget if budget is not None else data.budget)
@@ -34,15 +47,45 @@ class DeviceLayer:
         self.sel_count = torch.zeros((S, Hkv), dtype=torch.int32, device=self.device)
         self.out = torch.zeros_like(data.q)
         self.stream = stream
-        self.full_ws = None
+        self._on = _as_stream(stream, self.device)
+        self._behind_current()
+        self.full_ws = None       # workspace of the last full_decode
+        self._full = []           # the layer's workspaces of full_decode,
+        self._graph_full = []     # and those that one captured call uses alone
+
+    def _behind_current(self):
+        """The layer's stream waits for what the current stream holds, the
+        fills of buffers just made among it."""
+        if self._on is not None:
+            cur = torch.cuda.current_stream(self.device)
+            if cur != self._on:
+                self._on.wait_stream(cur)
+
+    def _workspace(self, nbytes: int) -> torch.Tensor:
+        """A workspace made, filled and one day reused on the layer's stream."""
+        with torch.cuda.stream(self._on):
+            return abi.alloc_workspace(nbytes, self.device)
+
+    def _full_workspace(self, nbytes: int) -> torch.Tensor:
+        """A workspace of at least `nbytes`.  One that was handed out is never
+        dropped: calls in flight and captured graphs go on using it.  In a
+        capture that finds none, the fill would be part of the graph, so that
+        call gets one of its own."""
+        for ws in self._full:
+            if ws.numel() >= nbytes:
+                return ws
+        with torch.cuda.stream(self._on):
+            captured = torch.cuda.is_current_stream_capturing()
+        ws = self._workspace(nbytes)
+        (self._graph_full if captured else self._full).append(ws)
+        return ws
 
     # -- steps 1-2 --------------------------------------------------------
     def build_centroids(self, keep_ws: bool = False, fused: bool = False):
         """Steps 1-2: the separate build and quantize calls, or with `fused`
         the single call; both give the same bits."""
         if self.build_ws is None:
-            n = abi.absp_build_workspace_size(self.kv)
-            self.build_ws = abi.alloc_workspace(n, self.device)
+            self.build_ws = self._workspace(abi.absp_build_workspace_size(self.kv))
         if fused:
             abi.absp_build_quantize_centroids(self.kv, self.build_ws, self.cent, self.stream)
         else:
@@ -86,18 +129,24 @@ class DeviceLayer:
 
     # -- the whole cache: exact attention, accumulated weights, eviction ------
     def new_weights(self) -> torch.Tensor:
-        """Accumulated attention weights of the layer's tokens, all zero."""
+        """Accumulated attention weights of the layer's tokens, all zero, on
+        the layer's stream and the current one."""
         d = self.data
-        return torch.zeros((d.num_seqs, d.num_kv_heads, self.kv.c.max_pages_per_seq * abi.PAGE_SIZE),
-                           dtype=torch.float32, device=self.device)
+        with torch.cuda.stream(self._on):
+            w = torch.zeros((d.num_seqs, d.num_kv_heads, self.kv.c.max_pages_per_seq * abi.PAGE_SIZE),
+                            dtype=torch.float32, device=self.device)
+        if self._on is not None:
+            cur = torch.cuda.current_stream(self.device)
+            if cur != self._on:
+                cur.wait_stream(self._on)
+        return w
 
     def full_decode(self, q=None, out=None, weights=None, shared_tokens: int = 0):
         """Exact attention over every cached token; `weights` (new_weights)
         accumulates the step's attention weights in place.  shared_tokens:
         length of the prefix whose pages all sequences share."""
         need = abi.absp_full_workspace_size(self.kv, shared_tokens, weights is not None)
-        if self.full_ws is None or self.full_ws.numel() < need:
-            self.full_ws = abi.alloc_workspace(need, self.device)
+        self.full_ws = self._full_workspace(need)
         q = self.data.q if q is None else q
         out = self.out if out is None else out
         if shared_tokens:
@@ -113,7 +162,8 @@ class DeviceLayer:
         (build_centroids)."""
         d = self.data
         kept = torch.empty((d.num_seqs, d.num_kv_heads, keep), dtype=torch.int32, device=self.device)
-        ws = abi.alloc_workspace(abi.absp_evict_workspace_size(self.kv, keep), self.device)
+        self._behind_current()    # `kept` may be memory that the current stream still uses
+        ws = self._workspace(abi.absp_evict_workspace_size(self.kv, keep))
         abi.absp_evict(self.kv, weights, keep, protect, recent, d.page_table, weights, kept,
                        d.seq_lens, ws, self.stream)
         self.check(ws)
