@@ -171,9 +171,16 @@ class DeviceLayer:
 
     # -- device-side faults ------------------------------------------------
     def check(self, ws=None):
-        st, detail = abi.absp_check_device_error(self.ws if ws is None else ws, self.stream)
-        if st != abi.ABSP_OK:
-            raise abi.AbspError(st, f"device fault (unit {detail})")
+        """Waits for the layer's calls and raises a fault that one of them
+        reported: in `ws`, or in any workspace of the layer's decode and
+        full_decode calls (one fault per call of check; the others stay to be
+        read).  Not among them: the workspace of a full_decode that was
+        captured before the layer had one, whose error word each replay
+        starts anew (`full_ws` after the capture; check(that) after a replay)."""
+        for w in [self.ws, *self._full] if ws is None else [ws]:
+            st, detail = abi.absp_check_device_error(w, self.stream)
+            if st != abi.ABSP_OK:
+                raise abi.AbspError(st, f"device fault (unit {detail})")
 
     # -- views of the centroid store ----------------------------------------
     def codes_of(self, s: int, h: int, n: int) -> torch.Tensor:

@@ -158,6 +158,39 @@ def test_a_workspace_in_use_is_never_dropped(lib, monkeypatch, capturing):
         assert dl.full_ws.data_ptr() == big and len({p for p, _ in seen}) <= 4
 
 
+def test_check_reads_every_workspace_of_the_layer(lib, monkeypatch):
+    abi, pipeline = lib
+    d = _data()
+    FakeCuda(monkeypatch, abi)
+    dl = pipeline.DeviceLayer(d)
+    words = {}
+
+    def read(ws, stream):                 # reads a workspace's error word and clears it
+        return words.pop(ws.data_ptr(), (abi.ABSP_OK, 0))
+
+    monkeypatch.setattr(abi, "absp_check_device_error", read)
+    dl.check()
+    dl.full_decode()
+    small = dl.full_ws
+    dl.full_decode(shared_tokens=64)
+    assert dl.full_ws.data_ptr() != small.data_ptr()
+    for ws in (dl.ws, small, dl.full_ws):  # a fault from before the layer grew among them
+        words[ws.data_ptr()] = (abi.ABSP_ERR_DEVICE_FAULT, 3)
+        with pytest.raises(abi.AbspError) as e:
+            dl.check()
+        assert e.value.status == abi.ABSP_ERR_DEVICE_FAULT
+        dl.check()
+    for ws in (dl.ws, small, dl.full_ws):  # none is cleared unread
+        words[ws.data_ptr()] = (abi.ABSP_ERR_TIMEOUT, 1)
+    for _ in range(3):
+        with pytest.raises(abi.AbspError):
+            dl.check()
+    dl.check()
+    words[small.data_ptr()] = (abi.ABSP_ERR_DEVICE_FAULT, 0)
+    dl.check(dl.full_ws)                  # one workspace alone
+    assert words
+
+
 # -------------------------------------------------------------------- GPU --
 
 def _f64(t):
@@ -268,3 +301,24 @@ def test_a_graph_outlives_a_growing_layer(lib, warm):
         st.synchronize()
         assert torch.equal(dl.out.view(torch.int16), ref.view(torch.int16))
         dl.check(graph_ws)
+
+
+@pytest.mark.gpu
+def test_check_raises_a_fault_of_the_whole_cache_call(lib):
+    abi, pipeline = lib
+    d = _data("cuda")
+    dl = pipeline.DeviceLayer(d)
+    dl.full_decode()
+    dl.check()
+    page = int(d.page_table[1, 4])
+    d.page_table[1, 4] = 1 << 20
+    dl.full_decode()
+    dl.full_decode(weights=dl.new_weights(), shared_tokens=64)   # another workspace, the same fault
+    for _ in range(2):
+        with pytest.raises(abi.AbspError) as e:
+            dl.check()
+        assert e.value.status == abi.ABSP_ERR_DEVICE_FAULT
+    dl.check()
+    d.page_table[1, 4] = page
+    dl.full_decode()
+    dl.check()
