@@ -736,8 +736,9 @@ __global__ void __launch_bounds__(kMergeThreads)
                 e = ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - ms);
                 L = fmaf(ml.y, e, L);
             }
-            // eight parts' loads in flight; one that attended to nothing may
-            // hold anything
+            // eight parts' loads in flight.  Every part counts, one whose factor
+            // is 0 as well: a non-finite value in it reaches the output here
+            // as it does inside a part
             const int m = min(32, n - i0);
             for (int k0 = sub; k0 < m; k0 += 8 * per) {
                 float ek[8];
@@ -748,9 +749,9 @@ __global__ void __launch_bounds__(kMergeThreads)
                     ek[u] = __shfl_sync(0xffffffffu, e, k & 31);
                     const float* from = reinterpret_cast<const float*>(
                         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k & 31));
-                    if (k >= m) ek[u] = 0.0f;
-                    v[u] = ek[u] != 0.0f ? reinterpret_cast<const float4*>(from)[lane]
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k >= m) ek[u] = -1.0f;   // no part
+                    v[u] = !(ek[u] < 0.0f) ? reinterpret_cast<const float4*>(from)[lane]
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {

@@ -1,0 +1,70 @@
+"""Edges of the whole-cache operators that the main tests do not reach:
+non-finite values under a vanishing probability, the largest arguments,
+selections that mislead the eviction's sample, keys beyond its cache.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as CO
+from test_cache_ops_gpu import Case, _bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def abi():
+    from block_sparse_attention_kv_b200 import build
+    build.build()
+    from block_sparse_attention_kv_b200 import abi as m
+    return m
+
+
+def _at(c, s, t):
+    return int(c.table[s, t // 16]), t % 16
+
+
+def _point_at(c, s, t):
+    """Token t of sequence s takes every query's attention: its score lies
+    above any other by more than 500 (log2 units), so that whatever other
+    part of the cache a query meets joins with a factor that is 0 in fp32."""
+    q = c.q[s].float().view(c.Hkv, c.Hq // c.Hkv, 128)
+    page, slot = _at(c, s, t)
+    c.k[page, :, slot] = 150 * (q / q.norm(dim=-1, keepdim=True)).sum(1).bfloat16()
+
+
+@pytest.mark.parametrize("Hq", [8, 24])
+@pytest.mark.parametrize("wide", [False, True])
+def test_non_finite_values_under_a_vanishing_probability(abi, Hq, wide):
+    """An infinite or NaN value of an attended token makes its channel
+    non-finite wherever the sequence is cut, however small its probability."""
+    c = Case(abi, [3000, 70], Hq, 2, seed=61, gain=8.0, wide=wide)
+    _point_at(c, 0, 1234)
+    good = c.want()[0]
+    for t, ch, x in ((5, 3, np.inf), (1230, 11, -np.inf), (2100, 40, np.nan), (2999, 77, np.inf)):
+        page, slot = _at(c, 0, t)
+        c.v[page, :, slot, ch] = x
+    c.run()
+    c.check()
+    got = c.out.float().cpu().numpy()
+    odd = np.zeros(128, bool)
+    odd[[3, 11, 40, 77]] = True
+    assert not np.isfinite(got[0][:, odd]).any()
+    assert np.isfinite(got[0][:, ~odd]).all() and np.isfinite(got[1]).all()
+    assert np.abs(got[0][:, ~odd] - good[0][:, ~odd]).max() < 0.02
+
+
+@pytest.mark.parametrize("peak,odd_at", [(700, 100), (100, 700), (700, 639)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_non_finite_values_across_the_end_of_a_prefix(abi, peak, odd_at, wide):
+    c = Case(abi, [900 + i for i in range(5)], 8, 2, shared=640, seed=62, gain=8.0, wide=wide)
+    for s in range(5 if peak >= 640 else 1):
+        _point_at(c, s, peak)
+    page, slot = _at(c, 0, odd_at)
+    c.v[page, :, slot, 9] = np.inf
+    c.run()
+    c.check()
+    got = c.out.float().cpu().numpy()
+    assert not np.isfinite(got[0, :, 9]).any()
+    assert np.isfinite(np.delete(got[0], 9, axis=1)).all()
