@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_cluster_kernel(const
             }
         }
     } else {
-        for (int i = t0; i < keep; i += tn) kept[i] = i < len ? i : -1;
+        // (64 bits: the last step behind the largest keep passes 2^31)
+        for (int64_t i = t0; i < keep; i += tn) kept[i] = i < len ? static_cast<int32_t>(i) : -1;
         if (!alias)
             for (int i = t0; i < len; i += tn) w_out[i] = w_in[i];
     }
@@ -583,7 +584,8 @@ __global__ void __launch_bounds__(kOneThreads, 2) evict_select_one_kernel(const 
           }
         }
     } else {
-        for (int i = tid; i < keep; i += kOneThreads) kept[i] = i < len ? i : -1;
+        // (64 bits: the last step behind the largest keep passes 2^31)
+        for (int64_t i = tid; i < keep; i += kOneThreads) kept[i] = i < len ? static_cast<int32_t>(i) : -1;
         if (!alias)
             for (int i = tid; i < len; i += kOneThreads) w_out[i] = w_in[i];
     }

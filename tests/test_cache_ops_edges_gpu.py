@@ -68,3 +68,27 @@ def test_non_finite_values_across_the_end_of_a_prefix(abi, peak, odd_at, wide):
     got = c.out.float().cpu().numpy()
     assert not np.isfinite(got[0, :, 9]).any()
     assert np.isfinite(np.delete(got[0], 9, axis=1)).all()
+
+
+@pytest.mark.parametrize("pages", [20, 1100])
+def test_evict_with_the_largest_keep(abi, pages):
+    """keep_tokens 2^31 - 1: every token stays; pages: a block per unit, a cluster per unit."""
+    keep = 2 ** 31 - 1
+    c = Case(abi, [300], 1, 1, seed=63, max_pages=pages)
+    w = torch.rand((1, 1, c.cap), device="cuda")
+    w_out = torch.full_like(w, -3.0)
+    # a guard of one number behind the list (its length is odd)
+    kept = torch.full((keep + 1,), 5, dtype=torch.int32, device="cuda")
+    new = torch.zeros_like(c.d_lens)
+    k, v = c.k.clone(), c.v.clone()
+    ws = abi.alloc_workspace(abi.absp_evict_workspace_size(c.kv, keep), "cuda")
+    abi.absp_evict(c.kv, w, keep, 1000, 7, c.d_table, w_out, kept[:keep].view(1, 1, keep), new, ws)
+    assert abi.absp_check_device_error(ws) == (abi.ABSP_OK, 0)
+    assert new.tolist() == [300]
+    assert torch.equal(kept[:300], torch.arange(300, dtype=torch.int32, device="cuda"))
+    for a in range(300, keep, 1 << 28):
+        assert bool((kept[a:min(a + (1 << 28), keep)] == -1).all())
+    assert int(kept[keep]) == 5
+    assert torch.equal(w_out[..., :300], w[..., :300]) and bool((w_out[..., 300:] == -3.0).all())
+    assert torch.equal(c.k.view(torch.int16), k.view(torch.int16))
+    assert torch.equal(c.v.view(torch.int16), v.view(torch.int16))
