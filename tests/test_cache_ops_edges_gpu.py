@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from oracle import cache_oracle as CO
-from test_cache_ops_gpu import Case, _bits
+from test_cache_ops_gpu import Case, _bits, _evict_case, _run_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,94 @@ def test_evict_with_the_largest_keep(abi, pages):
     assert torch.equal(w_out[..., :300], w[..., :300]) and bool((w_out[..., 300:] == -3.0).all())
     assert torch.equal(c.k.view(torch.int16), k.view(torch.int16))
     assert torch.equal(c.v.view(torch.int16), v.view(torch.int16))
+
+
+# ------------------------------------------- the one-block selection's passes --
+
+ONE_WARPS = 16
+
+
+def _sampled(L):
+    """Positions whose keys the one-block selection's first pass counts: the
+    first of every four in the first 128 of every 512 of a warp's run."""
+    run = -(-L // (128 * ONE_WARPS)) * 128
+    p = np.arange(L)
+    in_run = p % run
+    return (in_run % 512 < 128) & (p % 4 == 0)
+
+
+def _keys(w):
+    u = (w + np.float32(0)).view(np.uint32)
+    return np.where(u >> 31 != 0, ~u, u | np.uint32(0x80000000)).astype(np.int64)
+
+
+def _sample_misses(w, L, keep, protect, recent):
+    """Whether the threshold lies outside the range that the sample suggests."""
+    mid = np.arange(protect, L - recent)
+    left = keep - protect - recent
+    k = _keys(w[:L])
+    s = np.sort(k[mid][_sampled(L)[mid]] >> 21)[::-1]
+    m = s.size
+    at, d = m * left / mid.size, 2 * np.sqrt(m) + 8
+    hi = (int(s[int(at - d) - 1]) << 21) + 0x1FFFFF if at > d + 1 else 1 << 40
+    lo = int(s[int(at + d) - 1]) << 21 if int(at + d) <= m else 0
+    threshold = np.sort(k[mid])[::-1][left - 1]
+    return not lo <= threshold <= hi
+
+
+def _check_evict(abi, c, w, dst, keep, protect, recent, alias):
+    before, wo, kept, new = _run_evict(abi, c, w, dst, keep, protect, recent, alias, alias)
+    k2, v2, wo2, kept2, new2 = CO.evict(w, c.lens, keep, protect, recent, before[0], before[1], c.table, dst,
+                                        before[2])
+    assert np.array_equal(kept, kept2) and np.array_equal(new, new2)
+    assert np.array_equal(wo.view(np.int32), wo2.view(np.int32))
+    assert np.array_equal(_bits(c.k), k2) and np.array_equal(_bits(c.v), v2)
+
+
+@pytest.mark.parametrize("high", [True, False])
+@pytest.mark.parametrize("where", ["fresh", "in_place"])
+def test_evict_when_the_sample_misleads(abi, high, where):
+    """Sampled positions hold the largest (smallest) weights: the threshold
+    lies outside the range that they bound, and every key is counted again."""
+    lens, keep, protect, recent = [6000, 4500, 300], 2500, 20, 100
+    c, w, dst = _evict_case(abi, lens, 2, keep, protect, recent, where, "normal", seed=64)
+    for s, L in enumerate(lens):
+        w[s, :, :L][:, _sampled(L)] += 1000 if high else -1000
+    for s in range(2):
+        for h in range(2):
+            assert _sample_misses(w[s, h], lens[s], keep, protect, recent)
+    _check_evict(abi, c, w, dst, keep, protect, recent, where == "in_place")
+
+
+@pytest.mark.parametrize("weights", ["normal", "ties", "odd", "misleading"])
+def test_evict_keys_beyond_the_blocks_cache(abi, weights):
+    """75 units of about 30,000 tokens: a block per unit, 24K keys of it in
+    shared memory and the rest read again in every pass.  The sequences list
+    the same source pages, as those of one prompt do."""
+    S, P, keep, protect, recent = 75, 1900, 3000, 17, 400
+    r = np.random.default_rng(65)
+    lens = [P * 16 - 23 * s for s in range(S - 2)] + [2900, 24 * 1024 + 1]
+    pk = -(-keep // 16)
+    perm = r.permutation(P + S * pk).astype(np.int32)
+    c = Case(abi, [1], 1, 1)
+    c.lens, c.S, c.cap = lens, S, P * 16
+    c.table = np.ascontiguousarray(np.broadcast_to(perm[:P], (S, P)))
+    dst = perm[P:].reshape(S, pk)
+    g = torch.Generator(device="cuda").manual_seed(66)
+    c.k = torch.randn((P + S * pk, 1, 16, 128), generator=g, device="cuda").bfloat16()
+    c.v = torch.randn((P + S * pk, 1, 16, 128), generator=g, device="cuda").bfloat16()
+    c.d_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    c.d_table = torch.from_numpy(c.table).cuda()
+    c.kv = abi.LayerKV(c.d_lens, c.d_table, c.k, c.v, [16], 1)
+    w = r.standard_normal((S, 1, c.cap)).astype(np.float32)
+    if weights == "ties":
+        w = np.round(2 * w)
+    elif weights == "odd":
+        w[r.random(w.shape) < 0.3] = np.nan
+        w[r.random(w.shape) < 0.05] = np.inf
+        w[r.random(w.shape) < 0.2] = -0.0
+    elif weights == "misleading":
+        for s, L in enumerate(lens):
+            w[s, :, :L][:, _sampled(L)] -= 1000
+        assert _sample_misses(w[0, 0], lens[0], keep, protect, recent)
+    _check_evict(abi, c, w, dst, keep, protect, recent, False)
