@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     f1 = min(f0 + chunk, total);
     if (lane == 0) sh.ends[warp] = RunEnds{-1, -1, nullptr, nullptr};
     }
+    bool gave_up = false;      // the same in every lane
     if (f0 < f1) {
 
     // the unit and page that run position f0 falls on
@@ -269,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
     const float qks = kLog2E / sqrtf(static_cast<float>(kD));
     int stage = 0, phase = 0;
-    uint64_t limit = kWaitLimitNs;
     int f = f0;
     while (f < f1 && up < un) {
         // ---- one unit, or the part of it in this run
@@ -295,10 +295,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             sc = p.ws.scores + (static_cast<int64_t>(us) * c.Hq + uh * c.G) * c.max_pages * kPage;
 
         for (; f < seg_end; ++f, ++up) {
-            if (!mbar_try_wait(bars + 8 * stage, phase)) {
-                mbar_wait_bounded(bars + 8 * stage, phase, p.ws.err, 16, limit);
-                // one wait that gave up (the error is recorded) is enough
-                if (!mbar_try_wait(bars + 8 * stage, phase)) limit = 1000;
+            if (!gave_up && __any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
+                mbar_wait_bounded(bars + 8 * stage, phase, p.ws.err, 16);
+                // a wait that gave up (the error is recorded) is the run's
+                // last: no further copies, what is left of the pages counts as
+                // bad, and copies under way are waited for before the end
+                if (__any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
+                    gave_up = true;
+                    pf = f1;
+                    okmask = 0;
+                }
             }
             const int tok0 = ustart + up * kPage;
             const int valid = (okmask >> stage) & 1u ? min(kPage, ulen - tok0) : 0;
@@ -466,6 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             do un = own_pages(c, ++us, p.ws.err, &ustart, &ulen); while (un == 0 && us + 1 < c.S);
         }
     }
+    }
+    if (gave_up) {
+        // copies in flight end well within this time
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 10000000ull) {
+        }
     }
     __syncthreads();
 
