@@ -18,7 +18,6 @@ struct CacheDesc {
     int32_t S, Hq, Hkv, G;
     int32_t max_pages;
     int32_t shared;               // tokens of the shared prefix (a multiple of 16), 0: none
-    int32_t pad_;
     int64_t num_phys_pages;
     const int32_t* seq_lens;
     const int32_t* page_table;

@@ -15,10 +15,11 @@
 //
 // What bounds it is moving the kept rows, 1 KiB read and written per token
 // and head in 256-byte pieces from anywhere in the pools.  Measured on a
-// B200: 32 x 32K tokens, 8 heads, cut to 4096 with 1024 in place (805 MB of
-// rows) 195 us: 58 of selection, 137 of rows at 5.9 TB/s (91 % of the
-// measured copy bandwidth); a ragged batch of 24 cut to 16383 475 us; one 32K
-// sequence cut to 8192 30 us (16 and 14).
+// B200: 32 x 32K tokens, 8 heads, cut to 4096 with the first 1024 where they
+// are (805 MB of rows) 193 us: 58 of selection, 137 of rows at 5.9 TB/s (91 %
+// of the measured copy bandwidth), 201 us with the page table itself as the
+// destination; a ragged batch of 24 cut to 16383 472 us; one 32K sequence cut
+// to 8192 30 us (16 and 14).
 #include <algorithm>
 #include <atomic>
 
@@ -539,49 +540,49 @@ __global__ void __launch_bounds__(kOneThreads, 2) evict_select_one_kernel(const 
         const uint32_t below = (1u << lane) - 1u;
 #pragma unroll 1
         for (int j0 = i0; j0 < i1; j0 += 512) {
-          uint4 k4[4];
-          fetch(j0 + 4 * lane, false, k4);
+            uint4 k4[4];
+            fetch(j0 + 4 * lane, false, k4);
 #pragma unroll
-          for (int step = 0; step < 4; ++step) {         // every lane takes part
-            const int i = j0 + 128 * step + 4 * lane;
-            if (j0 + 128 * step >= i1) break;
-            uint32_t u = 0, q = 0;
-            if (i < i1) {
-                const uint4 k = k4[step];
-                u = (k.x > prefix ? 1u : 0u) | (k.y > prefix ? 2u : 0u) | (k.z > prefix ? 4u : 0u) |
-                    (k.w > prefix ? 8u : 0u);
-                q = (k.x == prefix ? 1u : 0u) | (k.y == prefix ? 2u : 0u) | (k.z == prefix ? 4u : 0u) |
-                    (k.w == prefix ? 8u : 0u);
-            }
-            if (__any_sync(0xffffffffu, q != 0)) {       // ties join in order while some are wanted
+            for (int step = 0; step < 4; ++step) {       // every lane takes part
+                const int i = j0 + 128 * step + 4 * lane;
+                if (j0 + 128 * step >= i1) break;
+                uint32_t u = 0, q = 0;
+                if (i < i1) {
+                    const uint4 k = k4[step];
+                    u = (k.x > prefix ? 1u : 0u) | (k.y > prefix ? 2u : 0u) | (k.z > prefix ? 4u : 0u) |
+                        (k.w > prefix ? 8u : 0u);
+                    q = (k.x == prefix ? 1u : 0u) | (k.y == prefix ? 2u : 0u) | (k.z == prefix ? 4u : 0u) |
+                        (k.w == prefix ? 8u : 0u);
+                }
+                if (__any_sync(0xffffffffu, q != 0)) {       // ties join in order while some are wanted
+                    uint32_t before = 0, all = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t m = __ballot_sync(0xffffffffu, q >> e & 1);
+                        before += __popc(m & below);
+                        all += __popc(m);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (q >> e & 1) {
+                            if (before < ties) u |= 1u << e;
+                            ++before;
+                        }
+                    ties -= min(ties, all);
+                }
                 uint32_t before = 0, all = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, q >> e & 1);
+                    const uint32_t m = __ballot_sync(0xffffffffu, u >> e & 1);
                     before += __popc(m & below);
                     all += __popc(m);
                 }
+                uint32_t r = at + before;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (q >> e & 1) {
-                        if (before < ties) u |= 1u << e;
-                        ++before;
-                    }
-                ties -= min(ties, all);
+                    if (u >> e & 1) kept[r++] = i + e;
+                at += all;
             }
-            uint32_t before = 0, all = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t m = __ballot_sync(0xffffffffu, u >> e & 1);
-                before += __popc(m & below);
-                all += __popc(m);
-            }
-            uint32_t r = at + before;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (u >> e & 1) kept[r++] = i + e;
-            at += all;
-          }
         }
     } else {
         // (64 bits: the last step behind the largest keep passes 2^31)
@@ -676,13 +677,15 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, int s, int h, cons
     move_batch((lane < 16 ? p.k_pages : p.v_pages) + (lane & 15) * 8, src, to, 0, between);
 }
 
-// Every row on its own, a warp per `ranks` (8, 16 or 32) ranks of one unit.  The
-// warps of a block
-// take the heads of a sequence side by side: the same ranks of its heads go to
-// the same pages and come from nearby ones, so a block's address translations
-// are shared by its warps (pages lie anywhere in pools of gigabytes).  A unit
-// with a destination page that is its own source page is compacted by its
-// first warp alone, in order.
+// Every row on its own, a warp per `ranks` (8, 16 or 32) ranks of one unit.
+// The warps of a block take the heads of a sequence side by side: the same
+// ranks of its heads go to the same pages and come from nearby ones, so a
+// block's address translations are shared by its warps (pages lie anywhere in
+// pools of gigabytes).  The bound of 64 registers spills eight words of set-up
+// per thread.  A unit with a destination page, behind the protected ones, that
+// is its own source page is compacted by its first warp alone, in order, eight
+// rows per round trip: 1.4 ms for 32 x 32K tokens cut to 4096, where
+// evict_compact_kernel takes 0.2 ms, 3.1 ms for one sequence cut to 8192.
 __global__ void __launch_bounds__(kCopyThreads, 4)
     evict_copy_kernel(const EvictArgs p, const int groups, const int ranks) {
     const CacheDesc& c = p.c;

@@ -23,8 +23,8 @@
 // 128-row tcgen05 tile would be mostly padding.  Measured on a B200, whole
 // call: 96 x 16K tokens, 2 KV heads of 16 query heads (1.61 GB) 267 us, 6.0
 // TB/s, 93 % of the measured copy bandwidth; a ragged batch of 32 with
-// weights (1.68 GB and 0.1 GB of scores) 309 us, 84 %; one 32K sequence with
-// weights (136 MB) 32.2 us, 66 %: about 19 us of streaming, the rest the
+// weights (1.68 GB and 0.1 GB of scores) 308 us, 84 %; one 32K sequence with
+// weights (136 MB) 32.0 us, 66 %: about 19 us of streaming, the rest the
 // dependent steps before it (lengths, page ids) and behind it (merge).
 #include <algorithm>
 #include <atomic>
@@ -165,313 +165,312 @@ __global__ void __launch_bounds__(kThreads, 1)
         up = f0;
         __syncthreads();   // the barriers are set up
     } else {
-    // cumulative own pages (per KV head) of the sequences; every step-th
-    // value stays in shared memory, block 0 writes all for the merge
-    step = (c.S + kCumCap - 1) / kCumCap;
-    int base = 0;
-    for (int s0 = 0; s0 < c.S; s0 += kThreads) {
-        const int s = s0 + tid;
-        int start, len;
-        const int n = s < c.S ? own_pages(c, s, p.ws.err, &start, &len) : 0;
-        int x = n;
+        // cumulative own pages (per KV head) of the sequences; every step-th
+        // value stays in shared memory, block 0 writes all for the merge
+        step = (c.S + kCumCap - 1) / kCumCap;
+        int base = 0;
+        for (int s0 = 0; s0 < c.S; s0 += kThreads) {
+            const int s = s0 + tid;
+            int start, len;
+            const int n = s < c.S ? own_pages(c, s, p.ws.err, &start, &len) : 0;
+            int x = n;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
+            for (int d = 1; d < 32; d *= 2) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) sh.warp_sum[warp] = x;
+            __syncthreads();
+            int before = base, all = 0;
+            for (int w = 0; w < kFullWarps; ++w) {
+                if (w < warp) before += sh.warp_sum[w];
+                all += sh.warp_sum[w];
+            }
+            if (s < c.S) {
+                if (s % step == 0) sh.cum[s / step] = before + x - n;
+                if (blockIdx.x == 0) p.ws.cum[s] = before + x - n;
+            }
+            base += all;
+            __syncthreads();
         }
-        if (lane == 31) sh.warp_sum[warp] = x;
-        __syncthreads();
-        int before = base, all = 0;
-        for (int w = 0; w < kFullWarps; ++w) {
-            if (w < warp) before += sh.warp_sum[w];
-            all += sh.warp_sum[w];
-        }
-        if (s < c.S) {
-            if (s % step == 0) sh.cum[s / step] = before + x - n;
-            if (blockIdx.x == 0) p.ws.cum[s] = before + x - n;
-        }
-        base += all;
-        __syncthreads();
-    }
-    if (blockIdx.x == 0 && tid == 0) p.ws.cum[c.S] = base;
-    const int total = base * c.Hkv;
-    const int chunk = (total + p.workers - 1) / p.workers;
-    f0 = static_cast<int>(min(static_cast<int64_t>(worker) * chunk, static_cast<int64_t>(total)));
-    f1 = min(f0 + chunk, total);
-    if (lane == 0) sh.ends[warp] = RunEnds{-1, -1, nullptr, nullptr};
+        if (blockIdx.x == 0 && tid == 0) p.ws.cum[c.S] = base;
+        const int total = base * c.Hkv;
+        const int chunk = (total + p.workers - 1) / p.workers;
+        f0 = static_cast<int>(min(static_cast<int64_t>(worker) * chunk, static_cast<int64_t>(total)));
+        f1 = min(f0 + chunk, total);
+        if (lane == 0) sh.ends[warp] = RunEnds{-1, -1, nullptr, nullptr};
     }
     bool gave_up = false;      // the same in every lane
     if (f0 < f1) {
-
-    // the unit and page that run position f0 falls on
-    if constexpr (!UNIT) {
-        int lo = 0, hi = (c.S - 1) / step;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (static_cast<int64_t>(sh.cum[mid]) * c.Hkv <= f0) lo = mid; else hi = mid - 1;
-        }
-        us = lo * step;
-        int before = sh.cum[lo];
-        un = own_pages(c, us, p.ws.err, &ustart, &ulen);
-        while (static_cast<int64_t>(before + un) * c.Hkv <= f0 && us + 1 < c.S) {
-            before += un;
-            un = own_pages(c, ++us, p.ws.err, &ustart, &ulen);
-        }
-        const int r = f0 - before * c.Hkv;
-        // (lengths that change during the call end the walk, not the bounds)
-        uh = min(r / max(un, 1), c.Hkv - 1);
-        up = r - uh * un;
-    }
-
-    const uint32_t ring_s = smem_u32(ring) + warp * kStages * kStageBytes;
-    uint8_t* ring_g = ring + warp * kStages * kStageBytes;
-    const uint32_t bars = smem_u32(&sh.bar[warp][0]);
-
-    // ---- producer: the same walk, kStages pages ahead
-    int ps = us, ph = uh, pp = up, pn = un, pstart = ustart, pf = f0;
-    int cbase = -64, my_phys = -1;   // page ids cbase .. cbase + 31 of the producer's unit
-    uint32_t okmask = 0;
-    // keys and values are read once: what stays in L2 is the scores
-    const uint64_t policy = evict_first_policy();
-    auto issue = [&](int st) {
-        if (pp >= cbase + 32 || pp < cbase) {
-            cbase = pp;
-            my_phys = pp + lane < pn
-                          ? c.page_table[static_cast<int64_t>(ps) * c.max_pages + pstart / kPage + pp + lane]
-                          : -1;
-        }
-        const int phys = __shfl_sync(0xffffffffu, my_phys, pp - cbase);
-        const bool ok = phys >= 0 && phys < c.num_phys_pages;
-        okmask = ok ? okmask | (1u << st) : okmask & ~(1u << st);
-        if (lane == 0) {
-            if (!ok) set_error(p.ws.err, ABSP_ERR_DEVICE_FAULT, ps);
-            const uint32_t bar = bars + 8 * st;
-            mbar_arrive_expect_tx(bar, ok ? kStageBytes : 0);
-            if (ok) {
-                const int y = (phys * c.Hkv + ph) * kPage;
-                tma_load_3d_hint(ring_s + st * kStageBytes, &tmk, 0, y, 0, bar, policy);
-                tma_load_3d_hint(ring_s + st * kStageBytes + kSlice, &tmv, 0, y, 0, bar, policy);
+        // the unit and page that run position f0 falls on
+        if constexpr (!UNIT) {
+            int lo = 0, hi = (c.S - 1) / step;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (static_cast<int64_t>(sh.cum[mid]) * c.Hkv <= f0) lo = mid; else hi = mid - 1;
             }
-        }
-        ++pf;
-        if (++pp == pn && pf < f1) {
-            pp = 0;
-            cbase = -64;
-            if (++ph == c.Hkv) {
-                ph = 0;
-                int len;
-                do pn = own_pages(c, ++ps, p.ws.err, &pstart, &len); while (pn == 0 && ps + 1 < c.S);
+            us = lo * step;
+            int before = sh.cum[lo];
+            un = own_pages(c, us, p.ws.err, &ustart, &ulen);
+            while (static_cast<int64_t>(before + un) * c.Hkv <= f0 && us + 1 < c.S) {
+                before += un;
+                un = own_pages(c, ++us, p.ws.err, &ustart, &ulen);
             }
-        }
-    };
-    for (int st = 0; st < kStages; ++st)
-        if (pf < f1) issue(st);
-
-    const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
-    const float qks = kLog2E / sqrtf(static_cast<float>(kD));
-    int stage = 0, phase = 0;
-    int f = f0;
-    while (f < f1 && up < un) {
-        // ---- one unit, or the part of it in this run
-        const int seg_end = min(f1, f - up + un);
-        const bool cut_left = up != 0, cut_right = f - up + un > f1;
-        const __nv_bfloat16* qg = p.q + (static_cast<int64_t>(us) * c.Hq + uh * c.G) * kD;
-        uint32_t qx[8], qy[8], qz[8], qw[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            qx[j] = g < c.G ? ld_u32g(qg + g * kD + 16 * j + 2 * t4) : 0u;
-            qy[j] = g < c.G ? ld_u32g(qg + g * kD + 16 * j + 8 + 2 * t4) : 0u;
-            if constexpr (BIG) {
-                qz[j] = g + 8 < c.G ? ld_u32g(qg + (g + 8) * kD + 16 * j + 2 * t4) : 0u;
-                qw[j] = g + 8 < c.G ? ld_u32g(qg + (g + 8) * kD + 16 * j + 8 + 2 * t4) : 0u;
-            }
-        }
-        float o[16][4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m0 = -INFINITY, m8 = -INFINITY, l0 = 0.0f, l8 = 0.0f;
-        float* sc = nullptr;
-        if constexpr (WEIGHTS)
-            sc = p.ws.scores + (static_cast<int64_t>(us) * c.Hq + uh * c.G) * c.max_pages * kPage;
-
-        for (; f < seg_end; ++f, ++up) {
-            if (!gave_up && __any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
-                mbar_wait_bounded(bars + 8 * stage, phase, p.ws.err, 16);
-                // a wait that gave up (the error is recorded) is the run's
-                // last: no further copies, what is left of the pages counts as
-                // bad, and copies under way are waited for before the end
-                if (__any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
-                    gave_up = true;
-                    pf = f1;
-                    okmask = 0;
-                }
-            }
-            const int tok0 = ustart + up * kPage;
-            const int valid = (okmask >> stage) & 1u ? min(kPage, ulen - tok0) : 0;
-            const uint32_t kb = ring_s + stage * kStageBytes, vb = kb + kSlice;
-            if (valid > 0 && valid < kPage) {
-                // V rows past the end may hold anything: 0 * NaN is NaN
-                uint8_t* vg = ring_g + stage * kStageBytes + kSlice;
-                const int nz = (kPage - valid) * 16;
-                for (int i = lane; i < nz; i += 32) {
-                    const int row = valid + (i >> 4), half = (i >> 3) & 1;
-                    *reinterpret_cast<uint4*>(vg + half * 2048 + row * 128 + (i & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                __syncwarp();
-            }
-            const int ta = 2 * t4, tb = 8 + 2 * t4;
-            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-            if (valid > 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int tok = (mi >> 1) * 8 + ri, ch = (j & 3) * 2 + (mi & 1);
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4(kb + (j >> 2) * 2048 + tok * 128 + ((ch ^ ri) << 4), b0, b1, b2, b3);
-                    if constexpr (BIG) {
-                        mma_bf16(s0[0], s0[1], s0[2], s0[3], qx[j], qz[j], qy[j], qw[j], b0, b1);
-                        mma_bf16(s1[0], s1[1], s1[2], s1[3], qx[j], qz[j], qy[j], qw[j], b2, b3);
-                    } else {
-                        mma_bf16_top(s0[0], s0[1], qx[j], qy[j], b0, b1);
-                        mma_bf16_top(s1[0], s1[1], qx[j], qy[j], b2, b3);
-                    }
-                }
-            }
-            // rows g (and g + 8): log2 units, nothing past the end
-            auto row = [&](float a, float b, float cc, float d, int r, float& m, float& l, uint32_t& h0,
-                           uint32_t& h1, uint32_t& r0, uint32_t& r1) -> float {
-                const float x0 = ta < valid ? a * qks : -INFINITY;
-                const float x1 = ta + 1 < valid ? b * qks : -INFINITY;
-                const float x2 = tb < valid ? cc * qks : -INFINITY;
-                const float x3 = tb + 1 < valid ? d * qks : -INFINITY;
-                if constexpr (WEIGHTS) {
-                    if (r < c.G) {
-                        float* at = sc + static_cast<int64_t>(r) * c.max_pages * kPage + tok0;
-                        *reinterpret_cast<float2*>(at + ta) = make_float2(x0, x1);
-                        *reinterpret_cast<float2*>(at + tb) = make_float2(x2, x3);
-                    }
-                }
-                float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m, mx);
-                const float ms = mn == -INFINITY ? 0.0f : mn;
-                const float corr = exp2_approx(m - ms);
-                const float p0 = exp2_approx(x0 - ms), p1 = exp2_approx(x1 - ms);
-                const float p2 = exp2_approx(x2 - ms), p3 = exp2_approx(x3 - ms);
-                l = l * corr + ((p0 + p1) + (p2 + p3));
-                m = mn;
-                h0 = pack_bf16x2(p0, p1);
-                h1 = pack_bf16x2(p2, p3);
-                r0 = pack_bf16x2(p0 - bf16lo(h0), p1 - bf16hi(h0));
-                r1 = pack_bf16x2(p2 - bf16lo(h1), p3 - bf16hi(h1));
-                return corr;
-            };
-            uint32_t pa0, pa2, pr0, pr2, pa1 = 0u, pa3 = 0u, pr1 = 0u, pr3 = 0u;
-            const float corr0 = row(s0[0], s0[1], s1[0], s1[1], g, m0, l0, pa0, pa2, pr0, pr2);
-            float corr8 = corr0;
-            if constexpr (BIG)
-                corr8 = row(s0[2], s0[3], s1[2], s1[3], g + 8, m8, l8, pa1, pa3, pr1, pr3);
-            if (__any_sync(0xffffffffu, corr0 != 1.0f || corr8 != 1.0f)) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    o[i][0] *= corr0;
-                    o[i][1] *= corr0;
-                    o[i][2] *= corr8;
-                    o[i][3] *= corr8;
-                }
-            }
-            if (valid > 0) {
-#pragma unroll
-                for (int cc = 0; cc < 8; ++cc) {
-                    const int tok = (mi & 1) * 8 + ri, ch = (cc & 3) * 2 + (mi >> 1);
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_trans(vb + (cc >> 2) * 2048 + tok * 128 + ((ch ^ ri) << 4), b0, b1, b2, b3);
-                    float* oa = o[2 * cc];
-                    float* ob = o[2 * cc + 1];
-                    if constexpr (BIG) {
-                        mma_bf16(oa[0], oa[1], oa[2], oa[3], pa0, pa1, pa2, pa3, b0, b1);
-                        mma_bf16(ob[0], ob[1], ob[2], ob[3], pa0, pa1, pa2, pa3, b2, b3);
-                        mma_bf16(oa[0], oa[1], oa[2], oa[3], pr0, pr1, pr2, pr3, b0, b1);
-                        mma_bf16(ob[0], ob[1], ob[2], ob[3], pr0, pr1, pr2, pr3, b2, b3);
-                    } else {
-                        mma_bf16(oa[0], oa[1], oa[2], oa[3], pa0, pr0, pa2, pr2, b0, b1);
-                        mma_bf16(ob[0], ob[1], ob[2], ob[3], pa0, pr0, pa2, pr2, b2, b3);
-                    }
-                }
-            }
-            // the buffer's reads (and zeroing) before its next copy
-            if (pf < f1) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(stage);
-            }
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1;
-            }
+            const int r = f0 - before * c.Hkv;
+            // (lengths that change during the call end the walk, not the bounds)
+            uh = min(r / max(un, 1), c.Hkv - 1);
+            up = r - uh * un;
         }
 
-        // ---- the unit's result, or this run's part of it
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l8 += __shfl_xor_sync(0xffffffffu, l8, 1);
-        l8 += __shfl_xor_sync(0xffffffffu, l8, 2);
-        if constexpr (!BIG) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                o[i][0] += o[i][2];
-                o[i][1] += o[i][3];
+        const uint32_t ring_s = smem_u32(ring) + warp * kStages * kStageBytes;
+        uint8_t* ring_g = ring + warp * kStages * kStageBytes;
+        const uint32_t bars = smem_u32(&sh.bar[warp][0]);
+
+        // ---- producer: the same walk, kStages pages ahead
+        int ps = us, ph = uh, pp = up, pn = un, pstart = ustart, pf = f0;
+        int cbase = -64, my_phys = -1;   // page ids cbase .. cbase + 31 of the producer's unit
+        uint32_t okmask = 0;
+        // keys and values are read once: what stays in L2 is the scores
+        const uint64_t policy = evict_first_policy();
+        auto issue = [&](int st) {
+            if (pp >= cbase + 32 || pp < cbase) {
+                cbase = pp;
+                my_phys = pp + lane < pn
+                              ? c.page_table[static_cast<int64_t>(ps) * c.max_pages + pstart / kPage + pp + lane]
+                              : -1;
             }
-        }
-        const int unit = us * c.Hkv + uh;
-        const bool whole = !cut_left && !cut_right;
-        // a part that later copies of this run cannot overwrite stays in the
-        // warp's page buffers; an earlier one goes through the workspace
-        const bool at_end = UNIT || f == f1;
-        float* part = at_end ? reinterpret_cast<float*>(ring_g)
-                             : p.ws.scratch + static_cast<int64_t>(worker) * c.G * kD;
-        __syncwarp();   // every lane is done reading the pages
-        auto put = [&](int r, int e, float m, float l) {
-            if (r >= c.G) return;
-            if (!UNIT && whole && p.prefix_ctas == 0) {
-                const float rl = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-                __nv_bfloat16* to = p.out + (static_cast<int64_t>(us) * c.Hq + uh * c.G + r) * kD;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint32_t*>(to + 8 * i + 2 * t4) =
-                        pack_bf16x2(o[i][e] * rl, o[i][e + 1] * rl);
-            } else {
-                float* to = !UNIT && whole ? p.ws.o + (unit_slot(p, unit) * c.G + r) * kD : part + r * kD;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<float2*>(to + 8 * i + 2 * t4) = make_float2(o[i][e], o[i][e + 1]);
+            const int phys = __shfl_sync(0xffffffffu, my_phys, pp - cbase);
+            const bool ok = phys >= 0 && phys < c.num_phys_pages;
+            okmask = ok ? okmask | (1u << st) : okmask & ~(1u << st);
+            if (lane == 0) {
+                if (!ok) set_error(p.ws.err, ABSP_ERR_DEVICE_FAULT, ps);
+                const uint32_t bar = bars + 8 * st;
+                mbar_arrive_expect_tx(bar, ok ? kStageBytes : 0);
+                if (ok) {
+                    const int y = (phys * c.Hkv + ph) * kPage;
+                    tma_load_3d_hint(ring_s + st * kStageBytes, &tmk, 0, y, 0, bar, policy);
+                    tma_load_3d_hint(ring_s + st * kStageBytes + kSlice, &tmv, 0, y, 0, bar, policy);
+                }
             }
-            if (t4 == 0) {
-                if (!UNIT && whole)
-                    p.ws.ml[unit_slot(p, unit) * c.G + r] = make_float2(m, l);
-                else
-                    sh.ml[warp][UNIT || cut_left ? 0 : 1][r] = make_float2(m, l);
+            ++pf;
+            if (++pp == pn && pf < f1) {
+                pp = 0;
+                cbase = -64;
+                if (++ph == c.Hkv) {
+                    ph = 0;
+                    int len;
+                    do pn = own_pages(c, ++ps, p.ws.err, &pstart, &len); while (pn == 0 && ps + 1 < c.S);
+                }
             }
         };
-        put(g, 0, m0, l0);
-        if constexpr (BIG) put(g + 8, 2, m8, l8);
-        if (lane == 0) {
-            if (cut_left) {
-                sh.ends[warp].first_unit = unit;
-                sh.ends[warp].first = part;
-            } else if (cut_right) {
-                sh.ends[warp].last = part;
+        for (int st = 0; st < kStages; ++st)
+            if (pf < f1) issue(st);
+
+        const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
+        const float qks = kLog2E / sqrtf(static_cast<float>(kD));
+        int stage = 0, phase = 0;
+        int f = f0;
+        while (f < f1 && up < un) {
+            // ---- one unit, or the part of it in this run
+            const int seg_end = min(f1, f - up + un);
+            const bool cut_left = up != 0, cut_right = f - up + un > f1;
+            const __nv_bfloat16* qg = p.q + (static_cast<int64_t>(us) * c.Hq + uh * c.G) * kD;
+            uint32_t qx[8], qy[8], qz[8], qw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                qx[j] = g < c.G ? ld_u32g(qg + g * kD + 16 * j + 2 * t4) : 0u;
+                qy[j] = g < c.G ? ld_u32g(qg + g * kD + 16 * j + 8 + 2 * t4) : 0u;
+                if constexpr (BIG) {
+                    qz[j] = g + 8 < c.G ? ld_u32g(qg + (g + 8) * kD + 16 * j + 2 * t4) : 0u;
+                    qw[j] = g + 8 < c.G ? ld_u32g(qg + (g + 8) * kD + 16 * j + 8 + 2 * t4) : 0u;
+                }
             }
-            if (cut_right) sh.ends[warp].last_unit = unit;
+            float o[16][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+            float m0 = -INFINITY, m8 = -INFINITY, l0 = 0.0f, l8 = 0.0f;
+            float* sc = nullptr;
+            if constexpr (WEIGHTS)
+                sc = p.ws.scores + (static_cast<int64_t>(us) * c.Hq + uh * c.G) * c.max_pages * kPage;
+
+            for (; f < seg_end; ++f, ++up) {
+                if (!gave_up && __any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
+                    mbar_wait_bounded(bars + 8 * stage, phase, p.ws.err, 16);
+                    // a wait that gave up (the error is recorded) is the run's
+                    // last: no further copies, what is left of the pages counts as
+                    // bad, and copies under way are waited for before the end
+                    if (__any_sync(0xffffffffu, !mbar_try_wait(bars + 8 * stage, phase))) {
+                        gave_up = true;
+                        pf = f1;
+                        okmask = 0;
+                    }
+                }
+                const int tok0 = ustart + up * kPage;
+                const int valid = (okmask >> stage) & 1u ? min(kPage, ulen - tok0) : 0;
+                const uint32_t kb = ring_s + stage * kStageBytes, vb = kb + kSlice;
+                if (valid > 0 && valid < kPage) {
+                    // V rows past the end may hold anything: 0 * NaN is NaN
+                    uint8_t* vg = ring_g + stage * kStageBytes + kSlice;
+                    const int nz = (kPage - valid) * 16;
+                    for (int i = lane; i < nz; i += 32) {
+                        const int row = valid + (i >> 4), half = (i >> 3) & 1;
+                        *reinterpret_cast<uint4*>(vg + half * 2048 + row * 128 + (i & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
+                }
+                const int ta = 2 * t4, tb = 8 + 2 * t4;
+                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+                if (valid > 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int tok = (mi >> 1) * 8 + ri, ch = (j & 3) * 2 + (mi & 1);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4(kb + (j >> 2) * 2048 + tok * 128 + ((ch ^ ri) << 4), b0, b1, b2, b3);
+                        if constexpr (BIG) {
+                            mma_bf16(s0[0], s0[1], s0[2], s0[3], qx[j], qz[j], qy[j], qw[j], b0, b1);
+                            mma_bf16(s1[0], s1[1], s1[2], s1[3], qx[j], qz[j], qy[j], qw[j], b2, b3);
+                        } else {
+                            mma_bf16_top(s0[0], s0[1], qx[j], qy[j], b0, b1);
+                            mma_bf16_top(s1[0], s1[1], qx[j], qy[j], b2, b3);
+                        }
+                    }
+                }
+                // rows g (and g + 8): log2 units, nothing past the end
+                auto row = [&](float a, float b, float cc, float d, int r, float& m, float& l, uint32_t& h0,
+                               uint32_t& h1, uint32_t& r0, uint32_t& r1) -> float {
+                    const float x0 = ta < valid ? a * qks : -INFINITY;
+                    const float x1 = ta + 1 < valid ? b * qks : -INFINITY;
+                    const float x2 = tb < valid ? cc * qks : -INFINITY;
+                    const float x3 = tb + 1 < valid ? d * qks : -INFINITY;
+                    if constexpr (WEIGHTS) {
+                        if (r < c.G) {
+                            float* at = sc + static_cast<int64_t>(r) * c.max_pages * kPage + tok0;
+                            *reinterpret_cast<float2*>(at + ta) = make_float2(x0, x1);
+                            *reinterpret_cast<float2*>(at + tb) = make_float2(x2, x3);
+                        }
+                    }
+                    float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m, mx);
+                    const float ms = mn == -INFINITY ? 0.0f : mn;
+                    const float corr = exp2_approx(m - ms);
+                    const float p0 = exp2_approx(x0 - ms), p1 = exp2_approx(x1 - ms);
+                    const float p2 = exp2_approx(x2 - ms), p3 = exp2_approx(x3 - ms);
+                    l = l * corr + ((p0 + p1) + (p2 + p3));
+                    m = mn;
+                    h0 = pack_bf16x2(p0, p1);
+                    h1 = pack_bf16x2(p2, p3);
+                    r0 = pack_bf16x2(p0 - bf16lo(h0), p1 - bf16hi(h0));
+                    r1 = pack_bf16x2(p2 - bf16lo(h1), p3 - bf16hi(h1));
+                    return corr;
+                };
+                uint32_t pa0, pa2, pr0, pr2, pa1 = 0u, pa3 = 0u, pr1 = 0u, pr3 = 0u;
+                const float corr0 = row(s0[0], s0[1], s1[0], s1[1], g, m0, l0, pa0, pa2, pr0, pr2);
+                float corr8 = corr0;
+                if constexpr (BIG)
+                    corr8 = row(s0[2], s0[3], s1[2], s1[3], g + 8, m8, l8, pa1, pa3, pr1, pr3);
+                if (__any_sync(0xffffffffu, corr0 != 1.0f || corr8 != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        o[i][0] *= corr0;
+                        o[i][1] *= corr0;
+                        o[i][2] *= corr8;
+                        o[i][3] *= corr8;
+                    }
+                }
+                if (valid > 0) {
+#pragma unroll
+                    for (int cc = 0; cc < 8; ++cc) {
+                        const int tok = (mi & 1) * 8 + ri, ch = (cc & 3) * 2 + (mi >> 1);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4_trans(vb + (cc >> 2) * 2048 + tok * 128 + ((ch ^ ri) << 4), b0, b1, b2, b3);
+                        float* oa = o[2 * cc];
+                        float* ob = o[2 * cc + 1];
+                        if constexpr (BIG) {
+                            mma_bf16(oa[0], oa[1], oa[2], oa[3], pa0, pa1, pa2, pa3, b0, b1);
+                            mma_bf16(ob[0], ob[1], ob[2], ob[3], pa0, pa1, pa2, pa3, b2, b3);
+                            mma_bf16(oa[0], oa[1], oa[2], oa[3], pr0, pr1, pr2, pr3, b0, b1);
+                            mma_bf16(ob[0], ob[1], ob[2], ob[3], pr0, pr1, pr2, pr3, b2, b3);
+                        } else {
+                            mma_bf16(oa[0], oa[1], oa[2], oa[3], pa0, pr0, pa2, pr2, b0, b1);
+                            mma_bf16(ob[0], ob[1], ob[2], ob[3], pa0, pr0, pa2, pr2, b2, b3);
+                        }
+                    }
+                }
+                // the buffer's reads (and zeroing) before its next copy
+                if (pf < f1) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    issue(stage);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+
+            // ---- the unit's result, or this run's part of it
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l8 += __shfl_xor_sync(0xffffffffu, l8, 1);
+            l8 += __shfl_xor_sync(0xffffffffu, l8, 2);
+            if constexpr (!BIG) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i][0] += o[i][2];
+                    o[i][1] += o[i][3];
+                }
+            }
+            const int unit = us * c.Hkv + uh;
+            const bool whole = !cut_left && !cut_right;
+            // a part that later copies of this run cannot overwrite stays in the
+            // warp's page buffers; an earlier one goes through the workspace
+            const bool at_end = UNIT || f == f1;
+            float* part = at_end ? reinterpret_cast<float*>(ring_g)
+                                 : p.ws.scratch + static_cast<int64_t>(worker) * c.G * kD;
+            __syncwarp();   // every lane is done reading the pages
+            auto put = [&](int r, int e, float m, float l) {
+                if (r >= c.G) return;
+                if (!UNIT && whole && p.prefix_ctas == 0) {
+                    const float rl = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+                    __nv_bfloat16* to = p.out + (static_cast<int64_t>(us) * c.Hq + uh * c.G + r) * kD;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        *reinterpret_cast<uint32_t*>(to + 8 * i + 2 * t4) =
+                            pack_bf16x2(o[i][e] * rl, o[i][e + 1] * rl);
+                } else {
+                    float* to = !UNIT && whole ? p.ws.o + (unit_slot(p, unit) * c.G + r) * kD : part + r * kD;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        *reinterpret_cast<float2*>(to + 8 * i + 2 * t4) = make_float2(o[i][e], o[i][e + 1]);
+                }
+                if (t4 == 0) {
+                    if (!UNIT && whole)
+                        p.ws.ml[unit_slot(p, unit) * c.G + r] = make_float2(m, l);
+                    else
+                        sh.ml[warp][UNIT || cut_left ? 0 : 1][r] = make_float2(m, l);
+                }
+            };
+            put(g, 0, m0, l0);
+            if constexpr (BIG) put(g + 8, 2, m8, l8);
+            if (lane == 0) {
+                if (cut_left) {
+                    sh.ends[warp].first_unit = unit;
+                    sh.ends[warp].first = part;
+                } else if (cut_right) {
+                    sh.ends[warp].last = part;
+                }
+                if (cut_right) sh.ends[warp].last_unit = unit;
+            }
+            // next unit with pages
+            up = 0;
+            if (!UNIT && f < f1 && ++uh == c.Hkv) {
+                uh = 0;
+                do un = own_pages(c, ++us, p.ws.err, &ustart, &ulen); while (un == 0 && us + 1 < c.S);
+            }
         }
-        // next unit with pages
-        up = 0;
-        if (!UNIT && f < f1 && ++uh == c.Hkv) {
-            uh = 0;
-            do un = own_pages(c, ++us, p.ws.err, &ustart, &ulen); while (un == 0 && us + 1 < c.S);
-        }
-    }
     }
     if (gave_up) {
         // copies in flight end well within this time
