@@ -1,7 +1,8 @@
 """Device buffers + ABI calls for one layer (no arithmetic of its own).
 
 `DeviceLayer` owns the centroid store and the workspaces of one paged layer
-and exposes the five library steps; tests, the smoke check and the
+and exposes the five steps of the sparse path and the whole-cache calls
+(exact decode, shared prefix, eviction); tests, the smoke check and the
 benchmark all drive the library through it.
 """
 
@@ -144,7 +145,9 @@ class DeviceLayer:
     def full_decode(self, q=None, out=None, weights=None, shared_tokens: int = 0):
         """Exact attention over every cached token; `weights` (new_weights)
         accumulates the step's attention weights in place.  shared_tokens:
-        length of the prefix whose pages all sequences share."""
+        length of the prefix whose pages all sequences share.  A call of its
+        kind ahead of a graph capture lets the captured ones share the layer's
+        workspace, which check() reads."""
         need = abi.absp_full_workspace_size(self.kv, shared_tokens, weights is not None)
         self.full_ws = self._full_workspace(need)
         q = self.data.q if q is None else q

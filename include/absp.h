@@ -362,7 +362,9 @@ ABSP_API absp_status absp_build_quantize_noalloc(const absp_layer_kv* kv,
 /* Workspace bytes of absp_full_decode (shared_tokens = 0) and
  * absp_shared_decode for this layer and shared_tokens; with_weights != 0
  * when the calls pass weights_out (it then holds the scores of one step,
- * 4 bytes per token and query head).  Host only, no launch.  A workspace
+ * 4 bytes per slot of the page table and query head, however long the
+ * sequences are: 1 GB for 64 sequences of 32 heads with tables for 131072
+ * tokens).  Host only, no launch.  A workspace
  * serves one call at a time: calls whose GPU work can overlap need one
  * each (also graphs that hold such calls). */
 ABSP_API absp_status absp_full_workspace_size(const absp_layer_kv* kv, int32_t shared_tokens,
@@ -430,7 +432,11 @@ ABSP_API absp_status absp_evict_workspace_size(const absp_layer_kv* kv, int32_t 
  * Destination pages: entry i of a row is either the sequence's own source
  * page i (compaction in place: dst_page_table may be kv->page_table with
  * dst_max_pages = kv->max_pages_per_seq) or a page that no sequence reads
- * as a source and no other entry names.  Pages of protected tokens are not
+ * as a source and no other entry names.  Compaction is fast where the table
+ * is kv->page_table itself; through another table that names a source page
+ * behind the protected ones (a copy of the page table, or a partly protected
+ * page left in place) each (sequence, head) concerned is moved by one warp,
+ * seven to seventy times slower.  Pages of protected tokens are not
  * written where they stay (protect_tokens whole pages, dst entry = source
  * page), so a prefix that sequences share may be protected and stays
  * shared.  keep_tokens >= 1, protect_tokens + recent_tokens <= keep_tokens.
