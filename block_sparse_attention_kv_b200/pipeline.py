@@ -15,12 +15,13 @@ from . import abi
 
 def _as_stream(stream, device):
     """torch's Stream for a stream argument: a Stream, a raw handle (0: the
-    legacy default stream) or None."""
-    if not isinstance(stream, int):
+    legacy default stream), an object that holds one as `cuda_stream`, or None."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
         return stream
-    if stream == 0:
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle == 0:
         return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.ExternalStream(handle, device=device)
 
 
 class DeviceLayer:

@@ -7,6 +7,7 @@ left unordered would show in the results.
 """
 
 import contextlib
+import types
 
 import numpy as np
 import pytest
@@ -122,6 +123,7 @@ def test_uses_come_behind_fills(lib, monkeypatch):
     abi, pipeline = lib
     d = _data()
     f = FakeCuda(monkeypatch, abi)
+    monkeypatch.setattr(pipeline, "_as_stream", lambda stream, device: stream)
     _calls(pipeline.DeviceLayer(d, stream=f.layer))
     f.assert_ordered()
     # what a caller does next on its own stream comes behind the weights' fill
@@ -209,9 +211,9 @@ def _dirty(nbytes):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("given", ["stream", "handle", "holder"])
 @pytest.mark.parametrize("wide", [False, True])
-def test_side_stream_results(lib, raw, wide):
+def test_side_stream_results(lib, given, wide):
     abi, pipeline = lib
     d = _data("cuda", (900, 700, 330), 256)
     if wide:
@@ -222,7 +224,8 @@ def test_side_stream_results(lib, raw, wide):
     torch.cuda.synchronize()
     _dirty(64 << 20)
     _hold_current()
-    dl = pipeline.DeviceLayer(d, stream=st.cuda_stream if raw else st)
+    holder = types.SimpleNamespace(cuda_stream=st.cuda_stream)
+    dl = pipeline.DeviceLayer(d, stream={"stream": st, "handle": st.cuda_stream, "holder": holder}[given])
     q, kp, vp = _f64(d.q), _f64(d.k_pages), _f64(d.v_pages)
     total = np.zeros((3, 2, d.page_table.shape[1] * 16))
     w = None
